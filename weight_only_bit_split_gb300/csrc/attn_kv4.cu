@@ -35,7 +35,8 @@
 // every element down to 2^-28 of the largest.  A block's scale multiplies its
 // float32 sum.  A value's scale varies along the summed axis, so it goes into
 // the other operand: p * dv is a float32 product, rounded once to fp16 (half
-// an ulp, 2^-11; p <= 1, so it never overflows).  Maxima, sums and
+// an ulp, 2^-11; p <= 1, so it never overflows: a score is rounded before the
+// maximum is subtracted, however large both are).  Maxima, sums and
 // accumulators are float32.
 //
 // Work.  A CTA step is 128 tokens of one (sequence, cache head, row tile):
@@ -246,19 +247,17 @@ __device__ __forceinline__ void warp_step(const Stage<DB>& st, int lane, const u
   float mx[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    if (MASK) {
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[mt][nt][i] = out(mt, nt, i) ? -INFINITY : s[mt][nt][i];
-    }
+      for (int i = 0; i < 4; ++i) s[mt][nt][i] = out(mt, nt, i) ? -INFINITY : __fmul_rn(s[mt][nt][i], scale2[nt][i & 1]);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       float v = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-      mx[nt][c] = fmaxf(r.m[nt][c], v * scale2[nt][c]);    // scale2 > 0
+      mx[nt][c] = fmaxf(r.m[nt][c], v);
       grows |= mx[nt][c] > r.m[nt][c];
     }
   }
@@ -284,8 +283,8 @@ __device__ __forceinline__ void warp_step(const Stage<DB>& st, int lane, const u
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float m = MASK && r.m[nt][i & 1] == -INFINITY ? 0.f : r.m[nt][i & 1];
-      s[0][nt][i] = exp2_approx(fmaf(s[0][nt][i], scale2[nt][i & 1], -m));
-      s[1][nt][i] = exp2_approx(fmaf(s[1][nt][i], scale2[nt][i & 1], -m));
+      s[0][nt][i] = exp2_approx(__fsub_rn(s[0][nt][i], m));
+      s[1][nt][i] = exp2_approx(__fsub_rn(s[1][nt][i], m));
       r.l[nt][i & 1] += s[0][nt][i] + s[1][nt][i];
     }
   }
