@@ -1,4 +1,5 @@
-"""Attention over the 4-bit cache where scores and values span many powers of two."""
+"""Attention over the 4-bit cache where the products of a probability and a value's scale span many powers of two:
+one token that leads by far, small value scales, a large value that no query looks at."""
 import pytest
 import torch
 
@@ -23,6 +24,43 @@ def led_cache(g, n, dim, q, lead, value, sink):
         cache.kd[page[token], 0, slot[token]] = score / (7 * float(q.float().abs().sum()) * dim ** -0.5)
         cache.vd[page[token], 0, slot[token]] = scale
     return cache, table, lens
+
+
+def attend64(q, cache, table, n, seen):
+    """Output, probability-weighted |v|, and the largest product of a probability and a token's largest value scale
+    (2^-25 at least), of one query over the first ``seen`` tokens."""
+    k, v = (t[:seen, 0] for t in held(cache, table, 0, n))
+    t = torch.arange(seen, device=dev())
+    scale = cache.vd[table[0].long()[t // 64], 0, t % 64].double().abs().amax(-1).clamp(min=2.0 ** -25)
+    s = (k @ q.double()) * q.numel() ** -0.5
+    e = torch.exp(s - s.max())
+    return e @ v / e.sum(), e @ v.abs() / e.sum(), (e * scale).max() / e.sum()
+
+
+CASES = [   # tokens, L, group, dim, lead, value, sink
+    (32768, 1, 4, 128, 12.0, 0.05, 0.0), (32768, 1, 4, 128, 12.0, 0.005, 2.0 ** -24), (8192, 1, 8, 128, 12.0, 0.0005, 0.01),
+    (8192, 3, 5, 128, 12.0, 0.005, 0.0), (32768, 1, 4, 128, 25.0, 0.05, 0.0), (8192, 1, 1, 64, 12.0, 0.005, 0.001),
+    (32768, 2, 8, 64, 20.0, 0.02, 2.0 ** -20), (8192, 1, 4, 256, 12.0, 0.005, 0.0), (32768, 2, 16, 256, 18.0, 0.05, 0.0),
+    (8192, 1, 4, 128, 0.0, 2.0 ** -18, 2.0 ** -18), (500, 1, 4, 128, 12.0, 2.0 ** -18, 0.0), (32768, 1, 4, 128, 0.0, 8000.0, 8000.0),
+    (700, 1, 4, 128, 12.0, 30000.0, 60000.0),
+]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("n,L,group,dim,lead,value,sink", CASES)
+def test_products_over_many_powers_of_two(dtype, n, L, group, dim, lead, value, sink):
+    """Half an ulp of fp16 for a product, as much again for the exponential and the float32 sums.  The largest product
+    lies above 2^14, so a subnormal one is off by 2^-25 / 2^14 of the largest, eight times that with its code."""
+    g = gen(31)
+    q = randn(g, dim, dtype=dtype)
+    cache, table, lens = led_cache(g, n, dim, q, lead, value, sink)
+    out = wobs.wobs_attn_kv4(cache, q.expand(1, L, group, dim), table, lens, out_dtype=F32)
+    for i in range(L):
+        seen = n - L + i + 1
+        o, a, w = attend64(q, cache, table, n, seen)
+        bound = 2 * U[F16] * a + seen * 2.0 ** -36 * w + U[F32] * o.abs()
+        err = (out[0, i].double() - o).abs()
+        assert bool((err <= bound).all()), f"max error over bound {float((err / bound).max()):.3g}, of the output {float((err / o.abs()).max()):.3g}"
 
 
 @pytest.mark.parametrize("power", [10, 20, 24, 26, 28, 31, 40])

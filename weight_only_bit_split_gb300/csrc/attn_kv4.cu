@@ -1,10 +1,10 @@
 // Attention of the newest tokens over a paged 4-bit key/value cache.
 //
 //   s[j] = scale * sum_b dk[j][b] * sum_{e in b} q[e] (ck[j][e] - 8)
-//   p[j] = exp(s[j] - max s),  o[e] = sum_j p[j] dv[j][b(e)] (cv[j][e] - 8) / sum_j p[j]
+//   p[j] = exp(s[j] - m),  o[e] = sum_j p[j] dv[j][b(e)] (cv[j][e] - 8) / sum_j p[j]
 //
 // over the tokens j <= lens[b] - L + i of query i; a query without any gives
-// zeros.  One pass over the cache with a running maximum and sum.
+// zeros.  One pass over the cache with a running maximum m and sum.
 //
 // Layout.  The queries that share a cache head (L tokens x group heads) are
 // the rows of the problem; eight of them fill the narrow side (n) of an
@@ -34,10 +34,16 @@
 // that brings its largest element to [2^14, 2^15) and held in fp16: exact for
 // every element down to 2^-28 of the largest.  A block's scale multiplies its
 // float32 sum.  A value's scale varies along the summed axis, so it goes into
-// the other operand: p * dv is a float32 product, rounded once to fp16 (half
-// an ulp, 2^-11; p <= 1, so it never overflows: a score is rounded before the
-// maximum is subtracted, however large both are).  Maxima, sums and
-// accumulators are float32.
+// the other operand: p * dv is a float32 product, rounded once to fp16.  So
+// that this neither overflows nor loses a token beside one that leads by far,
+// what a row's exponentials are relative to is not its largest score but the
+// largest s + log2(dv) - 15 so far, dv a token's largest value scale: the
+// largest product lies next to 2^15, one down to 2^-29 of it is rounded by half
+// an ulp (2^-11), a smaller one by 2^-40 of the largest.  Scores are rounded
+// before anything is subtracted, the addition of log2(dv) - 15 (made to lie in
+// -40 .. 0) rounds upwards: so also where scores are so large that the addition
+// is lost, no product exceeds 2^15 (or a scale beyond that) and the leading
+// token's exponential is at least 1.  Maxima, sums and accumulators are float32.
 //
 // Work.  A CTA step is 128 tokens of one (sequence, cache head, row tile):
 // four warps of 32 tokens, each with its own cp.async ring and its own running
@@ -144,6 +150,23 @@ __device__ __forceinline__ void load_scales(const __half* p, float (&d)[DB]) {
   }
 }
 
+// log2 of the largest magnitude among DB fp16 scales, less 15, in -40 .. 0 (a
+// NaN counts as none: its products are NaN whatever they are relative to).
+template <int DB>
+__device__ __forceinline__ float log2_largest(const __half* p) {
+  __half2 h[DB / 2];
+  if constexpr (DB == 2) *reinterpret_cast<uint32_t*>(h) = *reinterpret_cast<const uint32_t*>(p);
+  else if constexpr (DB == 4) *reinterpret_cast<uint2*>(h) = *reinterpret_cast<const uint2*>(p);
+  else *reinterpret_cast<uint4*>(h) = *reinterpret_cast<const uint4*>(p);
+  __half2 m = __habs2(h[0]);
+#pragma unroll
+  for (int i = 1; i < DB / 2; ++i) m = __hmax2(m, __habs2(h[i]));
+  const float2 f = __half22float2(m);
+  float l;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l) : "f"(fmaxf(f.x, f.y)));
+  return fminf(fmaxf(l - 15.f, -40.f), 0.f);
+}
+
 // One warp's stage: 32 tokens in two groups of 16.
 template <int DB>
 struct alignas(128) Stage {
@@ -243,6 +266,13 @@ __device__ __forceinline__ void warp_step(const Stage<DB>& st, int lane, const u
   auto out = [&](int mt, int nt, int i) {
     return MASK && (token0 + 16 * mt + g + 8 * (i >> 1) >= seen[nt][i & 1] || ((bad >> (16 * mt)) & 1u));
   };
+  // the lane's own token's, then those of its scores' tokens
+  const float own = log2_largest<DB>(&st.vd[lane >> 4][(lane & 15) * DB]);
+  float lg[2][2];
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) lg[mt][h] = __shfl_sync(0xffffffffu, own, 16 * mt + 8 * h + g);
   bool grows = false;
   float mx[NT][2];
 #pragma unroll
@@ -253,7 +283,8 @@ __device__ __forceinline__ void warp_step(const Stage<DB>& st, int lane, const u
       for (int i = 0; i < 4; ++i) s[mt][nt][i] = out(mt, nt, i) ? -INFINITY : __fmul_rn(s[mt][nt][i], scale2[nt][i & 1]);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float v = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+      float v = fmaxf(fmaxf(__fadd_ru(s[0][nt][c], lg[0][0]), __fadd_ru(s[0][nt][c + 2], lg[0][1])),
+                      fmaxf(__fadd_ru(s[1][nt][c], lg[1][0]), __fadd_ru(s[1][nt][c + 2], lg[1][1])));
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
