@@ -460,8 +460,11 @@ WOBS_API int wobs_dequantize_q8_1(const void* xq, int M, int K, int dtype, void*
  * one captured graph serves every step: token t of sequence b lies in slot
  * t % page_size of page table[b][t / page_size], and lens[b] counts the
  * tokens held, the newest L of the call included.  Table entries past a
- * sequence's last page are not read.  page_size a positive multiple of 16;
- * dim 64, 128 or 256.  The struct itself is host memory.
+ * sequence's last page are not read.  Tokens at positions that a table has
+ * no entry for (lens[b] above max_pages * page_size) are left out: not
+ * written, read as zeros, not attended to; the others keep their positions.
+ * page_size a positive multiple of 16; dim 64, 128 or 256.  The struct
+ * itself is host memory.
  */
 typedef struct {
   uint8_t* kq;
@@ -493,7 +496,8 @@ WOBS_API int wobs_kv4_append(const wobs_kv4_cache* cache, int dtype, const void*
 /*
  * Reads the newest L tokens of every sequence back: (code - 8) * scale as a
  * float32 product, rounded once to dtype, into contiguous K and V
- * [B][L][heads][dim] (16-byte aligned); zeros at negative positions.
+ * [B][L][heads][dim] (16-byte aligned); zeros at positions that are negative
+ * or past the table.
  */
 WOBS_API int wobs_kv4_read(const wobs_kv4_cache* cache, const int32_t* table, int64_t ld_table,
                            int max_pages, const int32_t* lens, int B, int L, int dtype, void* K,

@@ -419,7 +419,7 @@ attn_kv4_kernel(Kv4Args c, AttnKv4Args a, int tiles, int page_shift) {
   const int per_seq = c.heads * tiles;
   int64_t total = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int n = b0 + lane < a.B ? steps_of(kv4_length(c, b0 + lane)) + kSegmentCost : 0;
+    const int n = b0 + lane < a.B ? steps_of(kv4_length(c, b0 + lane).held) + kSegmentCost : 0;
     total += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(n));
   }
   total *= per_seq;
@@ -429,7 +429,7 @@ attn_kv4_kernel(Kv4Args c, AttnKv4Args a, int tiles, int page_shift) {
   int b = 0;
   int64_t before = 0;                                   // units of the sequences in front of b
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int n = b0 + lane < a.B ? steps_of(kv4_length(c, b0 + lane)) + kSegmentCost : 0;
+    const int n = b0 + lane < a.B ? steps_of(kv4_length(c, b0 + lane).held) + kSegmentCost : 0;
     int run = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -461,7 +461,8 @@ attn_kv4_kernel(Kv4Args c, AttnKv4Args a, int tiles, int page_shift) {
   const int64_t vd_delta = reinterpret_cast<const uint8_t*>(c.vd) - reinterpret_cast<const uint8_t*>(c.kd);
 
   for (int64_t at = begin; at < end;) {
-    const int len = kv4_length(c, b);
+    const Kv4Length length = kv4_length(c, b);
+    const int len = length.held;
     const int nsteps = steps_of(len);
     const int units = nsteps + kSegmentCost;
     const int seg = static_cast<int>((at - before) / units);
@@ -613,10 +614,10 @@ attn_kv4_kernel(Kv4Args c, AttnKv4Args a, int tiles, int page_shift) {
       for (int x = 0; x < 2; ++x) {
         scale2[nt][x] = __shfl_sync(0xffffffffu, down, 8 * t + 4 * x);
         const int col = row0 + 8 * nt + 2 * t + x;      // rows past the last are computed and dropped
-        seen[nt][x] = col < rows ? max(0, len - a.L + col / a.group + 1) : len;
+        seen[nt][x] = col < rows ? min(len, max(0, length.given - a.L + col / a.group + 1)) : len;
       }
     }
-    const int all_see = max(0, len - a.L + row0 / a.group + 1);   // tokens that every row of the tile sees
+    const int all_see = min(len, max(0, length.given - a.L + row0 / a.group + 1));   // tokens that every row of the tile sees
     __syncthreads();
 
     Rows<DB, NT> r;

@@ -5,7 +5,7 @@
 // magnitude (the first on ties), q = clamp(roundf(x / d) + 8, 0, 15), 8 where
 // d is 0.  The newest L tokens of sequence b stand at lens[b] - L ..
 // lens[b] - 1; positions below 0 (a prompt shorter than L, padded in front)
-// are left out.
+// and past the sequence's table are left out.
 #include "kv4.cuh"
 
 namespace wobs {
@@ -140,9 +140,10 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(Kv4Args c, Kv4Sour
   const int b = blockIdx.y, nb = c.dim >> 5;
   pdl_launch_dependents();
   pdl_wait();
-  const int at = kv4_length(c, b) - L + p.tok;
+  const Kv4Length len = kv4_length(c, b);
+  const int at = len.given - L + p.tok;
   const Kv4Token token = kv4_token(c, max(at, 0));
-  const int page = p.in && at >= 0 ? kv4_page(c, b, token) : -1;
+  const int page = p.in && at >= 0 && at < len.held ? kv4_page(c, b, token) : -1;
   const bool in = page >= 0;
   float x[2][8];
 #pragma unroll
@@ -190,9 +191,10 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(Kv4Args c, int L, T*
   pdl_launch_dependents();
   pdl_wait();
   if (!p.in) return;
-  const int at = kv4_length(c, b) - L + p.tok;
+  const Kv4Length len = kv4_length(c, b);
+  const int at = len.given - L + p.tok;
   const Kv4Token token = kv4_token(c, max(at, 0));
-  const int page = at >= 0 ? kv4_page(c, b, token) : -1;
+  const int page = at >= 0 && at < len.held ? kv4_page(c, b, token) : -1;
   uint32_t w[2] = {0x88888888u, 0x88888888u};
   float d[2] = {0.f, 0.f};
   if (page >= 0) {

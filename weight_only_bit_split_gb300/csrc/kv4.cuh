@@ -11,16 +11,21 @@
 
 namespace wobs {
 
-// Tokens held of sequence b, in 0 .. max_pages * page; a length outside that
-// range is cut to it and recorded in the error word.
-__device__ __forceinline__ int kv4_length(const Kv4Args& c, int b) {
+// Tokens of sequence b: as many as its length says, and those of them that its
+// table has room for (0 .. max_pages * page); a length outside that range is
+// recorded in the error word.  Positions follow from the given length, so the
+// tokens past the table's end are the ones left out.
+struct Kv4Length {
+  int given, held;
+};
+__device__ __forceinline__ Kv4Length kv4_length(const Kv4Args& c, int b) {
   const int n = c.lens[b];
   const int64_t most = static_cast<int64_t>(c.max_pages) * c.page;
   if (n < 0 || n > most) {
     if (c.err) *c.err = kErrCacheIndex;
-    return n < 0 ? 0 : static_cast<int>(most);
+    return n < 0 ? Kv4Length{0, 0} : Kv4Length{n, static_cast<int>(most)};
   }
-  return n;
+  return {n, n};
 }
 
 // n / d, by a shift where the (uniform) d is a power of two.
