@@ -69,6 +69,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 struct Row {
   float best, bins;      // largest value; bins for each unit of x
   float c_hi, c_lo;      // log2(e) / temperature as a sum of two floats
+  float alive;           // below this e < 2^-36, which rounds to no mass
 };
 struct alignas(8) Mass {
   uint32_t hi;           // multiples of 2^-18
@@ -77,12 +78,13 @@ struct alignas(8) Mass {
   __device__ __forceinline__ u64 sum() const { return (static_cast<u64>(hi) << 17) + static_cast<u64>(static_cast<long long>(lo)); }
 };
 
-// exp((v - best) / T): the argument of the power of two is rounded once.
+// exp((v - best) / T), 0 below alive: the argument of the power of two is rounded
+// once.  Above alive it is finite, whatever the temperature (v - best is made so).
 __device__ __forceinline__ float weight(const Row& r, float v) {
-  const float d = v - r.best;
+  const float d = fmaxf(v - r.best, -3.402823466e38f);
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(d, r.c_hi, d * r.c_lo)));
-  return v == r.best ? 1.0f : e;
+  return v == r.best ? 1.0f : v >= r.alive ? e : 0.0f;
 }
 // e in [0, 1]: adding 2^5 rounds it to a multiple of 2^-18, adding 1.5 * 2^-12
 // the exact rest to one of 2^-35; both are read off the sums' bits.
@@ -425,18 +427,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
   }
   Row r;
   r.best = most;
+  if (!(most < INFINITY)) temperature = 1.0f;   // only the infinities have a mass, at any temperature
   constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = static_cast<float>(1.4426950408889634 - kLog2e);
   r.c_hi = kLog2e / temperature;
-  r.c_lo = r.c_hi < INFINITY ? (fmaf(-r.c_hi, temperature, kLog2e) + kLog2eRest) / temperature : 0.f;   // the exact remainder's share
+  // the exact remainder's share; at an infinite temperature (c_hi 0: all masses equal) and a tiny one there is none
+  r.c_lo = r.c_hi > 0.f && r.c_hi < INFINITY ? (fmaf(-r.c_hi, temperature, kLog2e) + kLog2eRest) / temperature : 0.f;
+  r.alive = r.best - 36.1f / r.c_hi;            // -infinity where every token has a mass
   // one width for all bins, over the values that have a mass: (best - x) / T up to 26, where e < 2^-36
   const float span = fminf(r.best - least, 26.f * temperature);
   r.bins = span > 0.f && span < INFINITY ? kBins / span : 0.f;
   if (!(r.bins < INFINITY)) r.bins = 0.f;
 
-  // below this e < 2^-36, which rounds to no mass: one comparison for what are most tokens of a peaked row
-  const float alive = r.best - 36.1f / r.c_hi;
+  // one comparison for what are most tokens of a peaked row
   histogram(cluster, s, sl, slice, k > 0, [&](float v, int, Mass& mass) -> int {
-    if (!(v >= alive) || !(v > -INFINITY)) return -1;
+    if (!(v >= r.alive) || !(v > -INFINITY)) return -1;
     mass = mass_of(weight(r, v));
     return mass.none() ? -1 : bin_of(r, v);
   });
