@@ -540,9 +540,10 @@ WOBS_API int wobs_attn_kv4(const wobs_kv4_cache* cache, int dtype, const void* Q
  *          counts as -infinity; tokens at -infinity are never drawn, and
  *          where a row holds a +infinity only those are.
  *   u      float [M] in [0, 1).  temperature float [M] (<= 0: the largest
- *          logit's token; +infinity: all alike), top_k int32 [M] (<= 0: off), top_p float [M]
- *          (>= 1: off), min_p float [M] (<= 0: off): device arrays, each may
- *          be NULL (1, off, off, off).
+ *          logit's token; +infinity: all alike), top_k int32 [M] (<= 0: off),
+ *          top_p float [M] (>= 1: off), min_p float [M] (<= 0: off; above 1
+ *          as 1): device arrays, each may be NULL (1, off, off, off).  A NaN
+ *          among them is a temperature of 0 or a filter that is off.
  *   token  int64 [M]: the token, -1 for a row that holds nothing but
  *          -infinity and NaN.  prob float [M] or NULL: its probability among
  *          the kept tokens (0 for such a row).

@@ -65,3 +65,21 @@ def randn_rows(g):
     x[:, 1::7] = -3.4e38
     x[:, [11, 700, 2000, 4999]] = 2e10
     return x
+
+
+def test_nan_parameters():
+    """A NaN temperature takes the largest logit's token, a NaN top_p or min_p leaves the filter off."""
+    x = peaked(gen(53), 5, 3000)
+    u = torch.tensor([0.05, 0.3, 0.5, 0.7, 0.95], device=dev())
+    nan = torch.full((5,), float("nan"), device=dev())
+    plain, chance = wobs.wobs_sample(x, u)
+    assert plain.tolist() != x.argmax(-1).tolist()
+    for filters in (dict(min_p=nan), dict(top_p=nan), dict(top_p=nan, min_p=nan)):
+        t, p = wobs.wobs_sample(x, u, **filters)
+        assert torch.equal(t, plain) and torch.equal(p, chance)
+    t, p = wobs.wobs_sample(x, u, temperature=nan, min_p=nan)
+    assert t.tolist() == x.argmax(-1).tolist() and p.tolist() == [1.0] * 5
+    half, _ = wobs.wobs_sample(x, u, min_p=torch.full((5,), 0.5, device=dev()))
+    mixed = torch.tensor([0.5, float("nan"), 0.5, float("nan"), -1.0], device=dev())
+    t, _ = wobs.wobs_sample(x, u, min_p=mixed)
+    assert t.tolist() == [int((half if i in (0, 2) else plain)[i]) for i in range(5)]

@@ -407,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
     o->least[rank] = least;
   }
   float temperature = a.temperature ? a.temperature[m] : 1.0f;
-  float min_e = a.min_p ? fminf(a.min_p[m], 1.0f) : 0.f;
+  const float given = a.min_p ? a.min_p[m] : 0.f;
+  float min_e = given > 0.f ? fminf(given, 1.0f) : 0.f;        // NaN: off
   const float p = a.top_p ? a.top_p[m] : 1.0f;
   const int k = a.top_k ? a.top_k[m] : 0;
   const bool greedy = !(temperature > 0.f);
