@@ -736,7 +736,8 @@ def wobs_attn_kv4(cache, q, table, lens, scale=None, out=None, out_dtype=None, w
 
     Causal: query i sees positions up to lens - L + i; one that sees none gives zeros.  q_heads is a
     multiple of the cache's heads (grouped heads).  ``scale`` defaults to dim ** -0.5.  Returns a
-    contiguous tensor of q's shape, of q's dtype or float32 (``out_dtype``).
+    contiguous tensor of q's shape, of q's dtype or float32 (``out_dtype``), which like a product's
+    output must not be the weights of a product among the library's next calls on the stream.
     """
     lib = _lib.get()
     index, B, table_ptr, pitch, P, lens_ptr = _sequences(cache, table, lens)

@@ -21,12 +21,17 @@ namespace wobs {
 //
 // Decode-path kernels are launched with programmatic stream serialisation:
 // a kernel may start while the previous kernel on the stream is finishing.
-// Before pdl_wait() a kernel only reads its weight planes (never written by
-// a decode-path kernel); activations, outputs and the workspace are touched
-// only after pdl_wait(), which returns once the previous kernel has
-// completed and its writes are visible.  Kernels that write weights (the
-// Q4_0 / NF4 quantisers) never call pdl_launch_dependents, so a GEMV right
-// after them starts only when they are done.
+// Before pdl_wait() a kernel only reads its weight planes; activations,
+// outputs and the workspace are touched only after pdl_wait(), which returns
+// once the previous kernel has completed and its writes are visible.  Kernels
+// whose outputs a product can take as weights (the Q4_0 / NF4 quantisers and
+// the NF4 dequantiser, the 4-bit cache's append and read-back, the Q8_1
+// dequantiser, the norm where it writes y or 16-bit sums) never call
+// pdl_launch_dependents, so a GEMV behind them starts only when they are done,
+// also where other kernels stand between.  The products and the attention do,
+// although their 16-bit outputs have the form of weights: callers are told not
+// to use those as W at once (held back, 131072 tokens of the cache cost 40.3 us
+// a call in a row of calls, 38.4 with successors that start early).
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() {

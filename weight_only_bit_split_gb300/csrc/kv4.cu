@@ -138,7 +138,6 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(Kv4Args c, Kv4Source<T> ks, Kv4Source<T> vs, int L) {
   const Place p = place_of<4>(c, L);
   const int b = blockIdx.y, nb = c.dim >> 5;
-  pdl_launch_dependents();
   pdl_wait();
   const Kv4Length len = kv4_length(c, b);
   const int at = len.given - L + p.tok;
@@ -188,7 +187,6 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(Kv4Args c, int L, T* __restrict__ ko, T* __restrict__ vo) {
   const Place p = place_of<8>(c, L);
   const int b = blockIdx.y, nb = c.dim >> 5;
-  pdl_launch_dependents();
   pdl_wait();
   if (!p.in) return;
   const Kv4Length len = kv4_length(c, b);
