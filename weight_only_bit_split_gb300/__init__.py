@@ -112,6 +112,7 @@ class StepGraph:
 # ------------------------------------------------------------ workspace
 
 _ws_cache = {}
+_ws_replaced = []     # outgrown ones: captured graphs may hold their addresses
 
 # Workspace bytes of the argmax state alone (counter, keys, alignment).  A
 # larger wobs_workspace_size() means the call splits K and needs the
@@ -128,11 +129,12 @@ def _auto_ws(op, M, N, K, device, argmax):
 def workspace(op, M, N, K, device=None):
     """A zero-filled workspace for (op, M, N, K) on the current stream.
 
-    Cached per (device, stream) and grown as needed; the library leaves its
-    counter region (the first WS_ZERO_BYTES bytes) zero after every
-    successful call and overwrites split-K partials before reading them, so
-    it is reused as is.  Calls
-    that may overlap on the GPU should run on different streams.
+    Cached per (device, stream) and grown as needed, twofold at least; an
+    outgrown one is kept, since a captured graph may still use it.  The
+    library leaves its counter region (the first WS_ZERO_BYTES bytes) zero
+    after every successful call and overwrites partials before reading them,
+    so it is reused as is.  Calls that may overlap on the GPU should run on
+    different streams.
     """
     device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     need = wobs_workspace_size(op, M, N, K)
@@ -141,7 +143,11 @@ def workspace(op, M, N, K, device=None):
     key = (device.index, torch.cuda.current_stream(device).cuda_stream)
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < need:
-        buf = torch.zeros(max(need, 4096), dtype=torch.uint8, device=device)
+        size = max(need, 4096)
+        if buf is not None:
+            _ws_replaced.append(buf)
+            size = max(size, 2 * buf.numel())
+        buf = torch.zeros(size, dtype=torch.uint8, device=device)
         _ws_cache[key] = buf
     return buf
 
