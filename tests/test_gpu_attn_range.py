@@ -76,3 +76,22 @@ def test_scores_so_large_that_nothing_can_be_added_to_them(power, dim):
     _, v = held(cache, table, 0, 300)
     out = wobs.wobs_attn_kv4(cache, q.expand(1, 1, 4, dim), table, lens, out_dtype=F32)
     assert bool(((out[0, 0].double() - v[5, 0]).abs() <= 2 * U[F16] * v[5, 0].abs()).all())
+
+
+@pytest.mark.parametrize("power", [100, 117, 118, 122, 126])
+@pytest.mark.parametrize("scale", [None, -0.5, 2.0 ** -20])
+def test_queries_at_the_end_of_bf16s_range(power, scale):
+    """Queries around 2^power against small keys: the scores are finite, and the largest (smallest, where the scale is
+    negative) score's value is the output."""
+    g = gen(33)
+    q = randn(g, 128).abs().clamp(0.5, 1.9).to(BF16)
+    cache, table, lens = led_cache(g, 300, 128, q, 0.0, 8.0, 8.0)
+    cache.kd.mul_(2.0 ** -8)
+    cache.kd[table[0, 0], 0, 9] = 0.0
+    cache.kd[table[0, 0], 0, 5] = (-1 if scale is not None and scale < 0 else 1) * 2.0 ** -12
+    q = (q.float() * 2.0 ** power).to(BF16)
+    k, v = held(cache, table, 0, 300)
+    scores = (k[:, 0] @ q.double()) * (128 ** -0.5 if scale is None else scale)
+    assert int(scores.argmax()) == 5 and float(scores.abs().max()) < 3e38
+    out = wobs.wobs_attn_kv4(cache, q.expand(1, 1, 4, 128), table, lens, scale=scale, out_dtype=F32)
+    assert bool(((out[0, 0].double() - v[5, 0]).abs() <= 2 * U[F16] * v[5, 0].abs()).all())

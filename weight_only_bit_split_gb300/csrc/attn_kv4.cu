@@ -608,8 +608,9 @@ attn_kv4_kernel(Kv4Args c, AttnKv4Args a, int tiles, int page_shift) {
         if (DB < 8 && t == p + DB / 2) off[0][nt] = pack_half2(lo[2 * p], lo[2 * p + 1]);
         if (DB == 8 && t == p) off[1][nt] = pack_half2(lo[2 * p], lo[2 * p + 1]);
       }
-      // log2(e) and the powers of two; a scale of 0 has made the queries 0
-      const float down = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * 1.44269504088896341f * (0x1p24f / pow2);
+      // log2(e) and the powers of two (finite also for queries past 2^117, whose scores then
+      // are further apart than any exponential tells); a scale of 0 has made the queries 0
+      const float down = fminf((a.scale == 0.f ? 1.f : fabsf(a.scale)) * (1.44269504088896341f * 0x1p24f) / pow2, 3.402823466e38f);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         scale2[nt][x] = __shfl_sync(0xffffffffu, down, 8 * t + 4 * x);
