@@ -470,8 +470,8 @@ WOBS_API int wobs_dequantize_q8_1(const void* xq, int M, int K, int dtype, void*
  * sequence's last page are not read.  Tokens at positions that a table has
  * no entry for (lens[b] above max_pages * page_size) are left out: not
  * written, read as zeros, not attended to; the others keep their positions.
- * page_size a positive multiple of 16; dim 64, 128 or 256.  The struct
- * itself is host memory.
+ * page_size a positive multiple of 16, max_pages * page_size at most
+ * 2^31 - 1024; dim 64, 128 or 256.  The struct itself is host memory.
  */
 typedef struct {
   uint8_t* kq;

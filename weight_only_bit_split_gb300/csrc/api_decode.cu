@@ -44,6 +44,9 @@ int check_cache(const char* op, const wobs_kv4_cache* c, int B, int L, const int
     return fail(WOBS_ERR_UNSUPPORTED_SHAPE, "%s: dim=%d (64, 128 or 256)", op, c->dim);
   if (static_cast<double>(c->heads) * c->page_size * c->dim > 2147483647.0)
     return fail(WOBS_ERR_UNSUPPORTED_SHAPE, "%s: a page of more than 2^31 elements", op);
+  // positions are 32-bit, those of the steps that a kernel looks ahead among them
+  if (static_cast<int64_t>(max_pages) * c->page_size > (1ll << 31) - 1024)
+    return fail(WOBS_ERR_UNSUPPORTED_SHAPE, "%s: %d pages of %d tokens a sequence, more than 2^31 - 1024", op, max_pages, c->page_size);
   if (!aligned(c->kq, 16) || !aligned(c->vq, 16) || !aligned(c->kd, 16) || !aligned(c->vd, 16))
     return fail(WOBS_ERR_MISALIGNED, "%s: cache planes must be 16-byte aligned", op);
   if (!aligned(table, 4) || !aligned(lens, 4)) return fail(WOBS_ERR_MISALIGNED, "%s: table / lens not 4-byte aligned", op);
