@@ -31,11 +31,12 @@
  *     reported on return; results are ready when the stream reaches them.
  *     Any output may be any later call's input, with one exception: a
  *     product reads its first weights while the calls in front of it
- *     finish, so what a product (Y) or wobs_attn_kv4 (O) has written in
- *     16 bits may be its W only behind work on the stream that is not a
- *     call of this library (a copy, another kernel, an event's wait).  What
- *     the quantisers, the dequantisers, wobs_kv4_append, wobs_kv4_read and
- *     wobs_rmsnorm_q8_1 write may be W at once.
+ *     finish, so activations that a product (Y), wobs_rmsnorm_q8_1 (Y,
+ *     residual_out) or wobs_attn_kv4 (O) has written may be its W only
+ *     behind work on the stream that is not a call of this library (a copy,
+ *     another kernel, an event's wait).  What the quantisers, the
+ *     dequantisers, wobs_kv4_append and wobs_kv4_read write may be W at
+ *     once.
  *   - Activations and outputs with M columns are row-major [M][...]: column
  *     m of the mathematical X is the contiguous row X + m*ldx.
  *   - Weight matrices are row-major [N][K] (one output per row).

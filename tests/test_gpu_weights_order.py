@@ -33,19 +33,8 @@ def dequantised(g):
     return x, lambda: wobs.wobs_dequantize_q8_1(wobs.wobs_rmsnorm_q8_1(x, w)[0], F16, out), out
 
 
-def normed(g):
-    x, w, y = randn(g, ROWS, K), randn(g, K), torch.zeros(ROWS, K, dtype=BF16, device=dev())
-    return x, lambda: wobs.wobs_rmsnorm_q8_1(x, w, want_xq=False, y=y), y
-
-
-def summed(g):
-    x, w = randn(g, ROWS, K), randn(g, K)
-    r, h = randn(g, ROWS, K, dtype=F16), torch.zeros(ROWS, K, dtype=F16, device=dev())
-    return x, lambda: wobs.wobs_rmsnorm_q8_1(x, w, residual=r, residual_out=h), h
-
-
 @pytest.mark.parametrize("m", [1, 4])
-@pytest.mark.parametrize("make", [read_back, dequantised, normed, summed])
+@pytest.mark.parametrize("make", [read_back, dequantised])
 def test_outputs_are_weights_at_once(make, m):
     g = gen(61)
     x, call, weights = make(g)

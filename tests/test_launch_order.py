@@ -1,7 +1,7 @@
 """Which kernels let the next one on their stream start early (CPU only: the sources are read).
 
-A product copies its first weights before it waits for the kernels in front of it, so a kernel whose output can be a
-product's weights must not let its successors start."""
+A product copies its first weights before it waits for the kernels in front of it, so a kernel that writes a weight format,
+or a matrix out of one, must not let its successors start."""
 import os
 import re
 
@@ -35,8 +35,3 @@ def test_kernels_that_write_weights_hold_their_successors_back():
     for name in ("q4_0_quant_kernel", "nf4_quant_kernel", "nf4_dequant_kernel", "nf4_dequant_rows_kernel", "q8_1_dequant_kernel",
                  "kv4_append_kernel", "kv4_read_kernel"):
         assert calls(every[name]) == [], name
-
-
-def test_the_norm_holds_its_successors_back_behind_16_bit_outputs():
-    every = kernels()
-    assert calls(every["rmsnorm_q8_1_kernel"]) == ["if (!a.y && (!a.residual || sizeof(TR) == 4)) pdl_launch_dependents();"]

@@ -559,7 +559,8 @@ def wobs_rmsnorm_q8_1(x, weight, eps=1e-5, residual=None, residual_out=None, xq=
     ``residual`` itself); y = h / sqrt(mean(h^2) + eps) * weight in float32.  Returns (xq, h): the
     Q8_1 blocks of y (uint8 [M, K/32*36], None with ``want_xq=False``) and the stored sum (x itself
     without a residual).  ``y`` (float16, bfloat16 or float32 [M, K]) also receives y when given, for
-    products that take plain activations.
+    products that take plain activations (as their activations: a copy or another kernel must stand
+    between y or h and a product that takes them as weights).
     """
     lib = _lib.get()
     X2 = x if x.dim() == 2 else x.view(1, -1)
@@ -742,8 +743,8 @@ def wobs_attn_kv4(cache, q, table, lens, scale=None, out=None, out_dtype=None, w
 
     Causal: query i sees positions up to lens - L + i; one that sees none gives zeros.  q_heads is a
     multiple of the cache's heads (grouped heads).  ``scale`` defaults to dim ** -0.5.  Returns a
-    contiguous tensor of q's shape, of q's dtype or float32 (``out_dtype``), which like a product's
-    output must not be the weights of a product among the library's next calls on the stream.
+    contiguous tensor of q's shape, of q's dtype or float32 (``out_dtype``); as with every activation,
+    a copy or another kernel must stand between it and a product that takes it as weights.
     """
     lib = _lib.get()
     index, B, table_ptr, pitch, P, lens_ptr = _sequences(cache, table, lens)

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(most_threads(C), C == 2 ? 3 : 1) rmsnorm_q8_1_
   auto in = [&](int c) { return FULL || piece(c) < pieces; };   // all four lanes of a block agree: K is a multiple of 32
   float h[C][8];
   float sum = 0.f;
-  if (!a.y && (!a.residual || sizeof(TR) == 4)) pdl_launch_dependents();   // h and y may be the next product's weights
+  pdl_launch_dependents();
   pdl_wait();
   Raw8<TX> x[C];
   Raw8<TR> res[C];
