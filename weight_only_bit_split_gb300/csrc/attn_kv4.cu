@@ -37,10 +37,11 @@
 // the other operand: p * dv is a float32 product, rounded once to fp16.  So
 // that this neither overflows nor loses a token beside one that leads by far,
 // what a row's exponentials are relative to is not its largest score but the
-// largest s + log2(dv) - 15 so far, dv a token's largest value scale: the
-// largest product lies next to 2^15, one down to 2^-29 of it is rounded by half
-// an ulp (2^-11), a smaller one by 2^-40 of the largest.  Scores are rounded
-// before anything is subtracted, the addition of log2(dv) - 15 (made to lie in
+// largest s + e - 15 so far, 2^e the least power of two above a token's value
+// scales: the largest product lies in [2^14, 2^15), that token's products are
+// exact (its p is a power of two), others down to 2^-28 of the largest are
+// rounded by half an ulp (2^-11), smaller ones by 2^-39 of it.  Scores are
+// rounded before anything is subtracted, the addition of e - 15 (made to lie in
 // -40 .. 0) rounds upwards: so also where scores are so large that the addition
 // is lost, no product exceeds 2^15 (or a scale beyond that) and the leading
 // token's exponential is at least 1.  Maxima, sums and accumulators are float32.
@@ -150,10 +151,10 @@ __device__ __forceinline__ void load_scales(const __half* p, float (&d)[DB]) {
   }
 }
 
-// log2 of the largest magnitude among DB fp16 scales, less 15, in -40 .. 0 (a
-// NaN counts as none: its products are NaN whatever they are relative to).
+// e - 15 in -40 .. 0, where 2^e is the least power of two above the largest
+// magnitude among DB fp16 scales (a NaN's are NaN whatever this is).
 template <int DB>
-__device__ __forceinline__ float log2_largest(const __half* p) {
+__device__ __forceinline__ float log2_above(const __half* p) {
   __half2 h[DB / 2];
   if constexpr (DB == 2) *reinterpret_cast<uint32_t*>(h) = *reinterpret_cast<const uint32_t*>(p);
   else if constexpr (DB == 4) *reinterpret_cast<uint2*>(h) = *reinterpret_cast<const uint2*>(p);
@@ -162,9 +163,9 @@ __device__ __forceinline__ float log2_largest(const __half* p) {
 #pragma unroll
   for (int i = 1; i < DB / 2; ++i) m = __hmax2(m, __habs2(h[i]));
   const float2 f = __half22float2(m);
-  float l;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l) : "f"(fmaxf(f.x, f.y)));
-  return fminf(fmaxf(l - 15.f, -40.f), 0.f);
+  // the exponent's field behind that of 2^23
+  const float field = __uint_as_float(0x4B000000u | (__float_as_uint(fmaxf(f.x, f.y)) >> 23));
+  return fminf(fmaxf(field - (8388608.f + 127.f + 14.f), -40.f), 0.f);
 }
 
 // One warp's stage: 32 tokens in two groups of 16.
@@ -267,7 +268,7 @@ __device__ __forceinline__ void warp_step(const Stage<DB>& st, int lane, const u
     return MASK && (token0 + 16 * mt + g + 8 * (i >> 1) >= seen[nt][i & 1] || ((bad >> (16 * mt)) & 1u));
   };
   // the lane's own token's, then those of its scores' tokens
-  const float own = log2_largest<DB>(&st.vd[lane >> 4][(lane & 15) * DB]);
+  const float own = log2_above<DB>(&st.vd[lane >> 4][(lane & 15) * DB]);
   float lg[2][2];
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt)
