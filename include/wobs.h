@@ -516,10 +516,15 @@ WOBS_API int wobs_kv4_read(const wobs_kv4_cache* cache, const int32_t* table, in
  * query i of sequence b sees the tokens up to position lens[b] - L + i;
  * query heads h * group .. (h + 1) * group - 1 share cache head h, with
  * group = q_heads / heads.  O = softmax(scale * Q K^T) V; a query that sees
- * no token gives zeros.  The keys' codes are multiplied exactly (whole
- * numbers times fp16 or bf16 queries, float32 sums, scales applied in
- * float32); softmax statistics and sums are float32; the product of a
- * probability and a value's scale is rounded once to fp16.
+ * no token gives zeros.  A row of queries is scaled by a power of two and
+ * held in fp16: elements down to 2^-24 of its largest (bf16: 2^-27) exactly,
+ * smaller ones to within 2^-35 of the largest.  The keys' codes 0..15
+ * multiply them exactly, with float32 sums; the codes' offset, 8 times a
+ * block's sum of queries, is held as two fp16 numbers, to within 2^-15 of
+ * the row's largest query; the keys' scales are applied in float32.  Softmax
+ * statistics and sums are float32.  The product of a probability and a
+ * value's scale is rounded once to fp16, relative to the row's largest: half
+ * an ulp (2^-11) down to 2^-28 of that, 2^-39 of it below.
  *
  *   Q   [B][L][q_heads][dim] of dtype (fp16 or bf16), q_strides as above;
  *       1 <= L <= WOBS_MAX_M, q_heads a multiple of the cache's heads.

@@ -31,8 +31,13 @@
 // several tiles the codes, decoded once for all of them, become c - 8 first.
 //
 // Numbers.  A row of queries (fp16 or bf16) is multiplied by the power of two
-// that brings its largest element to [2^14, 2^15) and held in fp16: exact for
-// every element down to 2^-28 of the largest.  A block's scale multiplies its
+// that brings its largest element to [2^14, 2^15) and held in fp16; those that
+// meet the high codes carry 2^-4 more, so an fp16 element is exact down to
+// 2^-24 of the largest, a bf16 one down to 2^-27, and a smaller one is off by
+// 2^-35 of the largest at most: what a float32 sum with the largest loses is
+// 2^-24.  The offset's low half is an fp16 subnormal, its step 2^-24 of units in
+// which the largest query's part is 2^-7 or more: 2^-18 of that part is lost, far
+// below what P's rounding does to the output.  A block's scale multiplies its
 // float32 sum.  A value's scale varies along the summed axis, so it goes into
 // the other operand: p * dv is a float32 product, rounded once to fp16.  So
 // that this neither overflows nor loses a token beside one that leads by far,
@@ -395,11 +400,12 @@ constexpr int kNoPage = INT32_MIN;
 // ragged sequences; two: 125).  The larger accumulators need two.
 //
 // Measured on GB300 (dim 128, group 4, bf16): 32 sequences up to 32768, 607 MB:
-// 113.6 us, 5.3 TB/s, 79 % of the copy rate; one of 131072, 151 MB: 37.5 us, of
-// which 10 are its start and the join of 57 pieces a head; one of 1000: 8.6 us.
-// Bound by its chains of dependent instructions with three warps a scheduler (265
-// for 16 tokens of a head; issue 54 %, ALU pipe 45 %, tensor pipe 41 %), not yet
-// by DRAM: with the copies left out 112 us of then 117.
+// 117.4 us, 5.2 TB/s, 76 % of the copy rate; one of 131072, 151 MB: 38.3 us, of
+// which 10 are its start and the join of 57 pieces a head; one of 1000: 8.7 us.
+// Bound by its chains of dependent instructions with three warps a scheduler (280
+// for 16 tokens of a head, of which 16 keep the products of probabilities and
+// value scales in fp16's range: 114 us without; issue 56 %, ALU pipe 45 %, tensor
+// pipe 40 %), not yet by DRAM: with the copies left out 112 us of then 117.
 template <int DB, int NT>
 __global__ void __launch_bounds__(kThreads, DB * NT == 8 ? 2 : 3)
 attn_kv4_kernel(Kv4Args c, AttnKv4Args a, int tiles, int page_shift) {

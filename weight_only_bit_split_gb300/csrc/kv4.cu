@@ -132,8 +132,10 @@ __device__ __forceinline__ float largest_of_block(const float (&x)[8], int j) {
 
 // Four lanes a block, eight elements a lane, the keys and the values of the
 // same place.  Four prompts of 1500 tokens (8 heads of 128, fp16; 24.6 MB in,
-// 6.9 out): 10.2 us, 3.1 TB/s; bound by issue (the codes' arithmetic and the
-// places), 18.6 us with a division a code and by every index.
+// 6.9 out): 10.2 us, 3.1 TB/s; float32 13.4 us for 56 MB; bound by issue (the
+// codes' arithmetic and the places), 18.6 us with a division a code and by every
+// index.  The next kernel starts behind it, as behind the read-back: what they
+// write may be a product's weights.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(Kv4Args c, Kv4Source<T> ks, Kv4Source<T> vs, int L) {
   const Place p = place_of<4>(c, L);
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(Kv4Args c, Kv4Sour
 
 // Eight lanes a block, four elements a lane (a warp stores whole lines): (q - 8)
 // * d as a float32 product, rounded once to T.  The same tokens as float32 (6.9
-// MB in, 49 out): 12.1 us, 4.6 TB/s, where the output comes to DRAM; bound by its
+// MB in, 49 out): 12.4 us, 4.5 TB/s, where the output comes to DRAM; bound by its
 // stores and issue (four lanes a block and two 16-byte stores a lane: 2 us more).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(Kv4Args c, int L, T* __restrict__ ko, T* __restrict__ vo) {

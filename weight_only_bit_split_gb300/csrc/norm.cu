@@ -79,7 +79,9 @@ constexpr int most_threads(int C) { return C == 2 || C == 4 ? 512 : 1024; }
 // issued before the first is used.  TX, TR: types of x and of the residual.
 // Bound by DRAM latency between a row's phases: 2000 rows of 8192, bf16, 117 MB:
 // 23.8 us (4.9 TB/s); with four pieces a thread 24.6, of which 23.0 remain
-// without the quantiser and its stores.
+// without the quantiser and its stores.  Rows past 16384 take eight pieces a
+// thread, whose 64 registers spill: 250 rows of 65536, 51.7 us for the same 117
+// MB, against 36.3 for 1000 rows of 16384.
 // FULL: the threads' pieces are the row exactly.
 template <int C, bool FULL, typename TX, typename TR>
 __global__ void __launch_bounds__(most_threads(C), C == 2 ? 3 : 1) rmsnorm_q8_1_kernel(RmsNormArgs a) {
@@ -151,7 +153,8 @@ __global__ void __launch_bounds__(most_threads(C), C == 2 ? 3 : 1) rmsnorm_q8_1_
 }
 
 // Eight values a thread: q * d as a float32 product, rounded once to the
-// output's type.  2000 rows of 8192 to fp16 (18 MB in, 33 out): 8.9 us, 5.7 TB/s.
+// output's type.  2000 rows of 8192 to fp16 (18 MB in, 33 out): 9.0 us, 5.7 TB/s.
+// The next kernel starts behind it: what it writes may be a product's weights.
 __global__ void __launch_bounds__(256) q8_1_dequant_kernel(const uint8_t* __restrict__ xq, int64_t pieces,
                                                            int dtype, void* __restrict__ out) {
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;

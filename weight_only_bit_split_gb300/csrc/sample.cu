@@ -29,10 +29,12 @@
 //
 // Bound by latency for few rows (about ten dependent steps, four of them
 // barriers of the cluster): 1 row of 128000 float32 logits with every filter
-// 13.1 us, 32 rows 20.5 us (two CTAs an SM, one wave); by the same steps in
-// waves for many: 200 rows of 50257 bf16 logits 42.9 us.  All loops stay rolled: code that runs once a launch costs
-// the time to fetch it (slices in registers, 32 values unrolled in each pass:
-// 6 us a pass instead of 1.5).
+// 13.2 us, 32 rows 21.2 us (two CTAs an SM, one wave); by the same steps in
+// waves for many: 200 rows of 50257 bf16 logits 43.5 us.  The search by digits
+// costs a histogram for each digit: one row of 128000 equal logits 216 us, 200
+// rows of 50257 bf16 logits around 100 (some hundred values) 750 us.  All loops
+// stay rolled: code that runs once a launch costs the time to fetch it (slices in
+// registers, 32 values unrolled in each pass: 6 us a pass instead of 1.5).
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -46,7 +48,7 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 512;
 // 2^10 bins: with 2^11 peaked rows cost 8 % more (the bins' own work), flat ones
-// 12 % less (fewer tokens to sort): 1x128000 13.1 against 14.2 us, N(0, 1) alone 22.5 against 18.7
+// 17 % less (fewer tokens to sort): 1x128000 13.1 against 14.2 us, N(0, 1) alone 22.5 against 18.7
 constexpr int kBins = 1024, kDigit = 10;
 constexpr int kOwn = kBins / kThreads;   // consecutive bins of a thread
 constexpr int kSlice = 16383;      // tokens whose parts (at most 2^18, 2^16) 32-bit sums hold
