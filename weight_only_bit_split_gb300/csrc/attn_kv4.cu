@@ -36,11 +36,14 @@
 // 2^-24 of the largest, a bf16 one down to 2^-27, and a smaller one is off by
 // 2^-35 of the largest at most: what a float32 sum with the largest loses is
 // 2^-24.  The offset's low half is an fp16 subnormal, its step 2^-24 of units in
-// which the largest query's part is 2^-7 or more: 2^-18 of that part is lost, far
-// below what P's rounding does to the output.  A block's scale multiplies its
-// float32 sum.  A value's scale varies along the summed axis, so it goes into
-// the other operand: p * dv is a float32 product, rounded once to fp16.  So
-// that this neither overflows nor loses a token beside one that leads by far,
+// which the largest query's part is 2^-7 or more: 2^-18 of that part is lost at
+// most.  With one query of a row 30 times the others' and key scales around 10
+// the outputs' error stays P's (1.6e-5 of sum p |v|); at 1000 times it is 2.5e-4, of
+// which an offset held to 2^-22 (1 us of the 117 below) would take a quarter: the
+// rest is the float32 sums of codes eight above their values.  A block's scale
+// multiplies its float32 sum.  A value's scale varies along the summed axis, so
+// it goes into the other operand: p * dv is a float32 product, rounded once to
+// fp16.  So that this neither overflows nor loses a token beside one that leads by far,
 // what a row's exponentials are relative to is not its largest score but the
 // largest s + e - 15 so far, 2^e the least power of two above a token's value
 // scales: the largest product lies in [2^14, 2^15), that token's products are
